@@ -724,14 +724,19 @@ __device__ __forceinline__ void bound_mass(Shared& s, const uint4& cnt, float ta
   const uint32_t ic = block_scan<uint32_t>(c[0] + c[1] + c[2] + c[3], s.warp_u);
   if (threadIdx.x == 0) s.sel_bin[0] = s.sel_bin[1] = kBins;
   __syncthreads();
-  // a thousandth covers the rounding of the fp32 sums and of the bins' edges
+  // A thousandth covers the rounding of the fp32 sums and of the bins' edges.
+  // A thread's first bin that reaches the target, or none: the same numbers say
+  // both (id - sd + sd may round to less than id).
+  b0 = b1 = kBins;
 #pragma unroll
   for (int i = kPer - 1; i >= 0; --i) {
-    if (iu - su + up[i] >= target * 0.999f) b0 = kPer * (int)threadIdx.x + i;
-    if (id - sd + dn[i] >= target * 1.001f) b1 = kPer * (int)threadIdx.x + i;
+    if ((i == kPer - 1 ? iu : iu - su + up[i]) >= target * 0.999f)
+      b0 = kPer * (int)threadIdx.x + i;
+    if ((i == kPer - 1 ? id : id - sd + dn[i]) >= target * 1.001f)
+      b1 = kPer * (int)threadIdx.x + i;
   }
-  if (iu >= target * 0.999f) atomicMin(&s.sel_bin[0], b0);
-  if (id >= target * 1.001f) atomicMin(&s.sel_bin[1], b1);
+  if (b0 < kBins) atomicMin(&s.sel_bin[0], b0);
+  if (b1 < kBins) atomicMin(&s.sel_bin[1], b1);
   __syncthreads();
   b0 = s.sel_bin[0];
   b1 = s.sel_bin[1];
@@ -1282,7 +1287,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(SampleArgs a) {
       }
       set_scale(range);
       const float step = 1.44269504f / (T * scale);
-      int b0 = 0, b1 = 0;
+      int b0, b1;
       uint32_t upto;
       count_bins();
       bound_mass(s, c.end_round(), target, step, b0, b1, upto);
