@@ -136,6 +136,8 @@ def load(build_if_missing: bool = True):
             "vt_matmul_i8_workspace_size": ([], sz),
             "vt_matmul_i8": ([p, p, i32, p, p, i32, i32, p, p, i32, i64, p, sz,
                               p], ctypes.c_int),
+            "vt_selftest_matmul_i8": ([p, p, i32, p, p, i32, i32, p, p, i32, i64,
+                                       p, sz, i64, p], ctypes.c_int),
             "vt_sample_logits": ([p, i32, i32, i32, i64,
                                   ctypes.POINTER(SampleOptions), p, p, p, p, p,
                                   i64, p], ctypes.c_int),

@@ -53,6 +53,8 @@ vt_status matmul_i8_gemv(const I8Args& a, const DeviceInfo& di, cudaStream_t s);
 // shared memory as fp16, and few enough rows of W.
 bool matmul_i8_mma_fits(int M, int N, int d, const DeviceInfo& di);
 vt_status matmul_i8_mma(const I8Args& a, const DeviceInfo& di, cudaStream_t s);
-vt_status matmul_i8_tc(const I8Args& a, unsigned* err, const DeviceInfo& di, cudaStream_t s);
+// budget: clocks after which a wait gives up (0: its own limit, about a second).
+vt_status matmul_i8_tc(const I8Args& a, unsigned* err, long long budget, const DeviceInfo& di,
+                       cudaStream_t s);
 
 }  // namespace vt

@@ -46,7 +46,8 @@
 // 36.6 us, but M = 256 188 to 250).
 //
 // Waits on mbarriers are bounded; one that gives up records VT_ERR_TIMEOUT in
-// the error word, its CTA drains what it issued and frees its TMEM.
+// the error word and ends the CTA's other roles too; the loads and MMAs that the
+// CTA has issued are waited for before it frees its TMEM and leaves.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -72,7 +73,7 @@ constexpr int kMaxConv = 8;
 constexpr int kBlockM = 128;     // rows of X per block at most
 constexpr int kMaxRows = 1024;   // rows of X per launch
 constexpr int kMaxBlocks = kMaxRows / kBlockM;
-constexpr long long kWaitBudget = 2000000000LL;
+constexpr long long kWaitBudget = 2000000000LL;  // clocks
 
 // What the epilogue needs of a row of X: -128 times the sum of its bytes, and
 // its scale.
@@ -93,6 +94,7 @@ struct I8TcArgs {
   int splits, per;  // CTAs that share a tile's k, and the stages of each
   int stages, conv, accs;  // raw stages, converted buffers, accumulators
   unsigned* err;
+  long long budget;  // kShort: clocks after which a wait gives up
 };
 
 __device__ __forceinline__ void tmem_st_32x32_x8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -157,15 +159,31 @@ __device__ __forceinline__ bool try_wait_hint(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// mbarrier.test_wait, which never sleeps.
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // Bounded wait that also gives up once another role has.  Warps whose lanes
-// go on together vote on its result.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (try_wait_hint(bar, parity)) return true;
+// go on together vote on its result.  With kShort it gives up after `budget`
+// clocks and never sleeps.
+template <bool kShort>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         long long budget) {
+  auto done = [&]() { return kShort ? test_wait(bar, parity) : try_wait_hint(bar, parity); };
+  if (done()) return true;
   const long long t0 = clock64();
-  while (!try_wait_hint(bar, parity)) {
+  while (!done()) {
     if (*abort) return false;
-    if (clock64() - t0 > kWaitBudget) return false;
+    if (clock64() - t0 > (kShort ? budget : kWaitBudget)) return false;
   }
   return true;
 }
@@ -195,7 +213,9 @@ struct Ring {
 
 // kSplit, for few rows of W: a cluster's CTAs share a tile's k (one CTA may be
 // all of it), and blocks of X have CTAs of their own (blockIdx.y; mblocks is 1).
-template <bool kSplit>
+// kShort, for the self-test: waits of a.budget clocks (as a run-time limit in every
+// launch it cost 3 to 5 %: 256 x 128256 x 2048 190 to 199 us).
+template <bool kSplit, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_i8_tc_kernel(const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmX, I8TcArgs a) {
@@ -207,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t d_full[2], d_empty[2], drain, rows_full[kMaxBlocks];
   __shared__ uint32_t tmem_base;
   __shared__ volatile int abort_flag;
+  __shared__ int loads;  // stages whose loads have been issued
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this CTA's tiles, and its stages of each
@@ -248,6 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tensormap(&tmX);
   }
   for (int m = threadIdx.x; m < a.mblocks * a.nt; m += kThreads) rows[m].shift = 0;
+  auto await = [&](uint64_t* bar, uint32_t parity) {
+    return wait_bar<kShort>(bar, parity, &abort_flag, a.budget);
+  };
   auto load_stage = [&](int s, int tile, int mb, int kb) {
     uint8_t* st = smem + s * stage_bytes;
     tc::mbar_arrive_expect_tx(&raw_full[s], (uint32_t)stage_bytes);
@@ -284,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int mb = 0; ok && mb < a.mblocks; ++mb)
             for (int kb = 0; kb < nk; ++kb) {
               if (issued >= filled) {
-                if (!wait_bar(&raw_empty[r.i], r.ph ^ 1u, &abort_flag)) {
+                if (!await(&raw_empty[r.i], r.ph ^ 1u)) {
                   ok = false;
                   break;
                 }
@@ -293,18 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++issued;
               r.next(a.stages);
             }
-        if (!ok) {
-          give_up(a.err, &abort_flag);
-          // the last stages may still be landing
-          const int n = min(issued, a.stages);
-          for (int i = 0; i < n; ++i) {
-            if (--r.i < 0) {
-              r.i = a.stages - 1;
-              r.ph ^= 1u;
-            }
-            tc::mbar_wait(&raw_full[r.i], r.ph, kWaitBudget);
-          }
-        }
+        if (!ok) give_up(a.err, &abort_flag);
+        loads = issued;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- MMA issuer
@@ -319,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < nk; ++kb) {
             const bool first = kb % kChunkStages == 0;
             const bool last = kb % kChunkStages == kChunkStages - 1 || kb == nk - 1;
-            if (!__all_sync(~0u, (!first || wait_bar(&d_empty[d.i], d.ph ^ 1u, &abort_flag)) &&
-                                     wait_bar(&cv_full[c.i], c.ph, &abort_flag))) {
+            if (!__all_sync(~0u, (!first || await(&d_empty[d.i], d.ph ^ 1u)) &&
+                                     await(&cv_full[c.i], c.ph))) {
               ok = false;
               break;
             }
@@ -348,11 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             c.next(a.conv);
             if (last) d.next(a.accs);
           }
-      if (!ok && lane == 0) {
-        give_up(a.err, &abort_flag);
-        tc::mma_commit(&drain);
-        tc::mbar_wait(&drain, 0u, kWaitBudget);
-      }
+      if (!ok && lane == 0) give_up(a.err, &abort_flag);
       __syncwarp();
     }
   } else if (warp >= kConvA0 && warp < kConvA0 + 8 * a.subs) {
@@ -373,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bool ok = true;
     for (int i = u; i < total; i += 2) {
-      if (!__all_sync(~0u, wait_bar(&raw_full[r.i], r.ph, &abort_flag) &&
-                               wait_bar(&cv_empty[c.i], c.ph ^ 1u, &abort_flag))) {
+      if (!__all_sync(~0u, await(&raw_full[r.i], r.ph) &&
+                               await(&cv_empty[c.i], c.ph ^ 1u))) {
         ok = false;
         break;
       }
@@ -435,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = tile == tile0;
         int sum[kBlockM / 32] = {};
         for (; kb < nk; kb += 2) {
-          if (!__all_sync(~0u, wait_bar(&raw_full[r.i], r.ph, &abort_flag) &&
-                                   wait_bar(&cv_empty[c.i], c.ph ^ 1u, &abort_flag))) {
+          if (!__all_sync(~0u, await(&raw_full[r.i], r.ph) &&
+                                   await(&cv_empty[c.i], c.ph ^ 1u))) {
             ok = false;
             break;
           }
@@ -517,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 64; ++j) acc[j] = 0;
         for (int kb = 0; kb < nk; kb += kChunkStages) {
-          if (!__all_sync(~0u, wait_bar(&d_full[d.i], d.ph, &abort_flag))) {
+          if (!__all_sync(~0u, await(&d_full[d.i], d.ph))) {
             ok = false;
             break;
           }
@@ -549,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tc::mbar_arrive(&d_empty[d.i]);
           d.next(a.accs);
         }
-        if (ok && !__all_sync(~0u, wait_bar(&rows_full[mb], 0u, &abort_flag))) ok = false;
+        if (ok && !__all_sync(~0u, await(&rows_full[mb], 0u))) ok = false;
         if (splits > 1) {
           // every CTA's sums to the CTA that has their rows of X, which adds
           // them up (each warp of the cluster passes the barrier, whatever
@@ -620,6 +630,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     cl::sync();
   }
   __syncthreads();
+  if (abort_flag) {
+    // Some role gave up, whichever it was: loads and MMAs that nobody has waited
+    // for may still be under way.  The last load of each stage, and all MMAs: a
+    // commit covers the work of the thread that makes it, and elect.sync names
+    // the same lane every time.
+    if (threadIdx.x == 0)
+      for (int i = loads - min(loads, a.stages); i < loads; ++i)
+        tc::mbar_wait(&raw_full[i % a.stages], (uint32_t)(i / a.stages) & 1u, kWaitBudget);
+    if (warp == 1) {
+      if (elect_one()) {
+        tc::mma_commit(&drain);
+        tc::mbar_wait(&drain, 0u, kWaitBudget);
+      }
+      __syncwarp();
+    }
+  }
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
@@ -675,9 +701,9 @@ static int resident_clusters(int c, const DeviceInfo& di) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int active = 0;
-    if (cudaFuncGetAttributes(&fa, matmul_i8_tc_kernel<true>) != cudaSuccess) return 0;
+    if (cudaFuncGetAttributes(&fa, matmul_i8_tc_kernel<true, false>) != cudaSuccess) return 0;
     cfg.dynamicSmemBytes = di.max_smem_optin - fa.sharedSizeBytes;
-    if (cudaOccupancyMaxActiveClusters(&active, matmul_i8_tc_kernel<true>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&active, matmul_i8_tc_kernel<true, false>, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       return 0;
     }
@@ -686,13 +712,17 @@ static int resident_clusters(int c, const DeviceInfo& di) {
   return n;
 }
 
-static vt_status launch_tc(const I8Args& g, unsigned* err, const DeviceInfo& di, cudaStream_t s) {
-  if (!allow_max_smem(matmul_i8_tc_kernel<false>, di) ||
-      !allow_max_smem(matmul_i8_tc_kernel<true>, di))
+static vt_status launch_tc(const I8Args& g, unsigned* err, long long budget, const DeviceInfo& di,
+                           cudaStream_t s) {
+  if (!allow_max_smem(matmul_i8_tc_kernel<false, false>, di) ||
+      !allow_max_smem(matmul_i8_tc_kernel<true, false>, di) ||
+      (budget && (!allow_max_smem(matmul_i8_tc_kernel<false, true>, di) ||
+                  !allow_max_smem(matmul_i8_tc_kernel<true, true>, di))))
     return VT_ERR_CUDA;
   I8TcArgs a;
   a.g = g;
   a.err = err;
+  a.budget = budget;
   a.mblocks = (g.M + kBlockM - 1) / kBlockM;
   a.nt = ((g.M + a.mblocks - 1) / a.mblocks + 15) / 16 * 16;
   a.ntc = (a.nt + 31) / 32 * 32;
@@ -755,7 +785,9 @@ static vt_status launch_tc(const I8Args& g, unsigned* err, const DeviceInfo& di,
   CUtensorMap tmW, tmX;
   if (!byte_map(&tmW, g.W, g.N, g.d, a.rt) || !byte_map(&tmX, g.X, g.M, g.d, a.nt))
     return fail(VT_ERR_CUDA, "vt_matmul_i8: cuTensorMapEncodeTiled failed");
-  auto kernel = few ? matmul_i8_tc_kernel<true> : matmul_i8_tc_kernel<false>;
+  auto kernel = budget ? (few ? matmul_i8_tc_kernel<true, true> : matmul_i8_tc_kernel<false, true>)
+                       : few ? matmul_i8_tc_kernel<true, false>
+                             : matmul_i8_tc_kernel<false, false>;
   const int grid = std::min(a.ntiles, ways) * a.splits;
   const size_t smem = (size_t)a.stages * stage_bytes + b_bytes + 1024;
   cudaLaunchConfig_t cfg = {};
@@ -778,14 +810,15 @@ static vt_status launch_tc(const I8Args& g, unsigned* err, const DeviceInfo& di,
   return launch_status("matmul_i8_tc_kernel");
 }
 
-vt_status matmul_i8_tc(const I8Args& g, unsigned* err, const DeviceInfo& di, cudaStream_t s) {
+vt_status matmul_i8_tc(const I8Args& g, unsigned* err, long long budget, const DeviceInfo& di,
+                       cudaStream_t s) {
   for (int m = 0; m < g.M; m += kMaxRows) {
     I8Args p = g;
     p.M = std::min(kMaxRows, g.M - m);
     p.X = g.X + (int64_t)m * g.d;
     p.xs = g.xs + m;
     p.out = static_cast<char*>(g.out) + (int64_t)m * g.ldo * (g.out_bf16 ? 2 : 4);
-    const vt_status st = launch_tc(p, err, di, s);
+    const vt_status st = launch_tc(p, err, budget, di, s);
     if (st != VT_OK) return st;
   }
   return VT_OK;

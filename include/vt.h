@@ -555,6 +555,19 @@ vt_status vt_matmul_i8(const int8_t* X, const float* x_scale, int32_t M,
                        int32_t out_dtype, int64_t ldo, void* ws,
                        size_t ws_bytes, void* stream);
 
+/* vt_selftest_matmul_i8 — vt_matmul_i8 with waits of budget_cycles SM clock
+ * cycles at the most (1 .. 2^31) in place of about a second, to see its failure
+ * path work: a wait that runs out writes VT_ERR_TIMEOUT to the error word, the
+ * loads and products under way are waited for, and out is incomplete; where the
+ * word stays 0 out is the product.  For sizes whose kernel has such waits
+ * (more than 16 rows of X, or more than 4 with many rows of W); others are
+ * VT_ERR_UNSUPPORTED. */
+vt_status vt_selftest_matmul_i8(const int8_t* X, const float* x_scale, int32_t M,
+                                const int8_t* W, const float* w_scale, int32_t N,
+                                int32_t d, const float* bias, void* out,
+                                int32_t out_dtype, int64_t ldo, void* ws,
+                                size_t ws_bytes, int64_t budget_cycles, void* stream);
+
 /* ------------------------------------------------------------------------
  * vt_sample_logits — sampling with temperature, top-k, top-p and min-p from
  * given random numbers, and the distribution that is sampled from.  [VT]
