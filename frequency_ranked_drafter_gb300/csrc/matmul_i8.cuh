@@ -20,13 +20,14 @@ struct I8Args {
   int out_bf16;
 };
 
-// One output: the exact integer sum, rounded to fp32 once, then one rounding
+// One output, at i = m * ldo + n: the exact integer sum, rounded to fp32 once, then one rounding
 // each for the scales' product, the product with it and the bias; bf16 outputs
 // round once more.
 __device__ __forceinline__ void i8_store(const I8Args& a, int64_t i, int acc, float xs, float ws,
                                          float b) {
   float y = __fmul_rn(__int2float_rn(acc), __fmul_rn(xs, ws));
   if (a.bias) y = __fadd_rn(y, b);
+  if (!VT_CHECKED(i >= 0 && i < (a.M - 1) * a.ldo + a.N && i % a.ldo < a.N)) return;
   if (a.out_bf16)
     static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(y);
   else
