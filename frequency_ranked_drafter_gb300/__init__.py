@@ -539,16 +539,7 @@ def quantize_rows(X: torch.Tensor, ids: torch.Tensor | None = None,
     return (_ops or serving_ops()).quantize_rows(X, ids, out, scale, n_invalid)
 
 
-_i8_words: dict = {}  # per device: workspaces of matmul_i8 (its error word)
-
-
-def _i8_word(device: torch.device) -> torch.Tensor:
-    ws = torch.zeros(256, dtype=torch.uint8, device=device)
-    # a buffer made while a graph is captured belongs to that graph
-    if not torch.cuda.is_current_stream_capturing():
-        torch.cuda.current_stream(device).synchronize()  # zero for every stream
-        _i8_words[device] = ws
-    return ws
+_i8_words: dict = {}  # (device, stream): workspace of matmul_i8 (its error word)
 
 
 def matmul_i8(Q: torch.Tensor, scale: torch.Tensor, Wq: torch.Tensor,
@@ -560,15 +551,14 @@ def matmul_i8(Q: torch.Tensor, scale: torch.Tensor, Wq: torch.Tensor,
     and each channel: [M, N] = (Q . Wq^T, exact) * scale[m] * w_scale[n]
     + bias[n], fp32 or bf16.  ``out`` may have a row stride above N.
     ``check=True`` synchronises and raises VTError(VT_ERR_TIMEOUT) if a
-    bounded wait inside the kernels gave up."""
-    if ws is None:
-        if not isinstance(Q, torch.Tensor) or not Q.is_cuda:
-            raise TypeError("Q must be a CUDA tensor")
-        ws = _i8_words.get(Q.device)
-        if ws is None:
-            ws = _i8_word(Q.device)
-    y = (_ops or serving_ops()).matmul_i8(Q, scale, Wq, w_scale, bias, out, out_dtype, ws)
+    bounded wait inside the kernels gave up: in this call, or in an earlier one
+    with the same error word.  Calls share one word a stream; ``ws`` (256 zeroed
+    bytes) gives a call its own, for check_error_word to read later."""
+    y = (_ops or serving_ops()).matmul_i8(Q, scale, Wq, w_scale, bias, out, out_dtype, ws,
+                                          _i8_words)
     if check:
+        if ws is None:
+            ws = _i8_words[Q.device.index, _stream(Q.device)]
         check_error_word("vt_matmul_i8", ws)
     return y
 

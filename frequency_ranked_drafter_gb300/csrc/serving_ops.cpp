@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -28,6 +29,7 @@ namespace {
 struct Api {
   decltype(&vt_quantize_rows) quantize_rows;
   decltype(&vt_matmul_i8) matmul_i8;
+  decltype(&vt_matmul_i8_workspace_size) matmul_i8_workspace_size;
   decltype(&vt_sample_logits) sample_logits;
   decltype(&vt_verify_draft) verify_draft;
 } api;
@@ -181,9 +183,41 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// matmul_i8(Q, scale, Wq, w_scale, bias, out, out_dtype, ws)
+// The error word of this stream's calls without a workspace of their own, kept in
+// the dictionary `words` under (device, stream): a call that is checked then
+// sees (and clears) its own stream's word only.
+at::Tensor stream_word(PyObject* words, c10::Device dev, cudaStream_t stream) {
+  PyObject* key = Py_BuildValue("(iK)", (int)dev.index(),
+                                (unsigned long long)reinterpret_cast<uintptr_t>(stream));
+  if (!key) throw Refused();
+  PyObject* known = PyDict_GetItemWithError(words, key);  // borrowed
+  if (known) {
+    Py_DECREF(key);
+    return THPVariable_Unpack(known);
+  }
+  at::Tensor w;
+  int stored = -1;
+  if (!PyErr_Occurred()) {
+    w = at::zeros({(int64_t)api.matmul_i8_workspace_size()},
+                  at::TensorOptions().dtype(at::kByte).device(dev));
+    // a buffer made while a graph is captured belongs to that graph
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    C10_CUDA_CHECK(cudaStreamIsCapturing(stream, &status));
+    if (status != cudaStreamCaptureStatusNone) {
+      stored = 0;
+    } else if (PyObject* o = wrap(w)) {
+      stored = PyDict_SetItem(words, key, o);
+      Py_DECREF(o);
+    }
+  }
+  Py_DECREF(key);
+  if (stored < 0) throw Refused();
+  return w;
+}
+
+// matmul_i8(Q, scale, Wq, w_scale, bias, out, out_dtype, ws, words)
 PyObject* matmul_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     const at::Tensor& Q = cuda_tensor(a[0], "Q");
     const at::Tensor& W = cuda_tensor(a[2], "Wq");
     if (Q.dim() != 2 || W.dim() != 2) refuse(PyExc_ValueError, "Q and Wq must be 2-D");
@@ -209,14 +243,19 @@ PyObject* matmul_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ldo = row_stride(y, "out");
       want_place(y, "out", dev, {M, N});
     }
-    const at::Tensor& w = cuda_tensor(a[7], "ws");
-    dense(a[7], "ws", at::kByte, dev, {w.numel()});
     const c10::cuda::CUDAGuard guard(dev);
+    void* stream = stream_on(dev);
+    at::Tensor w;
+    if (a[7] == Py_None) {
+      w = stream_word(a[8], dev, static_cast<cudaStream_t>(stream));
+    } else {
+      w = cuda_tensor(a[7], "ws");
+      dense(a[7], "ws", at::kByte, dev, {w.numel()});
+    }
     done("vt_matmul_i8",
          api.matmul_i8(address<int8_t>(Q), xs, int32_of(M, "M"), address<int8_t>(W), ws,
                        int32_of(N, "N"), int32_of(d, "d"), bias, y.data_ptr(),
-                       element(y, "out", false), ldo, w.data_ptr(), (size_t)w.numel(),
-                       stream_on(dev)));
+                       element(y, "out", false), ldo, w.data_ptr(), (size_t)w.numel(), stream));
     return wrap(y);
   });
 }
@@ -350,9 +389,12 @@ PyObject* bind(PyObject*, PyObject* args) {
   }
   api.quantize_rows = reinterpret_cast<decltype(api.quantize_rows)>(dlsym(lib, "vt_quantize_rows"));
   api.matmul_i8 = reinterpret_cast<decltype(api.matmul_i8)>(dlsym(lib, "vt_matmul_i8"));
+  api.matmul_i8_workspace_size = reinterpret_cast<decltype(api.matmul_i8_workspace_size)>(
+      dlsym(lib, "vt_matmul_i8_workspace_size"));
   api.sample_logits = reinterpret_cast<decltype(api.sample_logits)>(dlsym(lib, "vt_sample_logits"));
   api.verify_draft = reinterpret_cast<decltype(api.verify_draft)>(dlsym(lib, "vt_verify_draft"));
-  if (!api.quantize_rows || !api.matmul_i8 || !api.sample_logits || !api.verify_draft) {
+  if (!api.quantize_rows || !api.matmul_i8 || !api.matmul_i8_workspace_size ||
+      !api.sample_logits || !api.verify_draft) {
     PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
     return nullptr;
   }
