@@ -539,7 +539,8 @@ def quantize_rows(X: torch.Tensor, ids: torch.Tensor | None = None,
     return (_ops or serving_ops()).quantize_rows(X, ids, out, scale, n_invalid)
 
 
-_i8_words: dict = {}  # (device, stream): workspace of matmul_i8 (its error word)
+# matmul_i8's workspaces (error words): (device, stream), captured calls (device, None)
+_i8_words: dict = {}
 
 
 def matmul_i8(Q: torch.Tensor, scale: torch.Tensor, Wq: torch.Tensor,
@@ -553,7 +554,8 @@ def matmul_i8(Q: torch.Tensor, scale: torch.Tensor, Wq: torch.Tensor,
     ``check=True`` synchronises and raises VTError(VT_ERR_TIMEOUT) if a
     bounded wait inside the kernels gave up: in this call, or in an earlier one
     with the same error word.  Calls share one word a stream; ``ws`` (256 zeroed
-    bytes) gives a call its own, for check_error_word to read later."""
+    bytes, kept while the call or its graph is in use) gives a call its own, for
+    check_error_word to read later: the way to learn of a timeout in replays."""
     y = (_ops or serving_ops()).matmul_i8(Q, scale, Wq, w_scale, bias, out, out_dtype, ws,
                                           _i8_words)
     if check:

@@ -11,7 +11,9 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/from_blob.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -183,35 +185,55 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A zeroed workspace of matmul_i8 that belongs to no graph, made while one is
+// captured: memory of its own (the allocator's would be the graph's, free for its
+// next tensor once nothing holds this one), zeroed now and not at each replay.
+at::Tensor word_beside_capture(c10::Device dev) {
+  const int64_t bytes = (int64_t)api.matmul_i8_workspace_size();
+  const c10::cuda::CUDAStreamCaptureModeGuard relaxed(cudaStreamCaptureModeRelaxed);
+  void* p = nullptr;
+  cudaStream_t side;
+  C10_CUDA_CHECK(cudaMalloc(&p, bytes));  // kept for the process
+  C10_CUDA_CHECK(cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking));
+  C10_CUDA_CHECK(cudaMemsetAsync(p, 0, bytes, side));
+  C10_CUDA_CHECK(cudaStreamSynchronize(side));
+  C10_CUDA_CHECK(cudaStreamDestroy(side));
+  return at::from_blob(p, {bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+}
+
 // The error word of this stream's calls without a workspace of their own, kept in
 // the dictionary `words` under (device, stream): a call that is checked then
-// sees (and clears) its own stream's word only.
+// sees (and clears) its own stream's word only.  Calls captured on a stream that
+// has none yet share one a device, under (device, None).
 at::Tensor stream_word(PyObject* words, c10::Device dev, cudaStream_t stream) {
   PyObject* key = Py_BuildValue("(iK)", (int)dev.index(),
                                 (unsigned long long)reinterpret_cast<uintptr_t>(stream));
   if (!key) throw Refused();
   PyObject* known = PyDict_GetItemWithError(words, key);  // borrowed
-  if (known) {
-    Py_DECREF(key);
-    return THPVariable_Unpack(known);
-  }
-  at::Tensor w;
-  int stored = -1;
-  if (!PyErr_Occurred()) {
-    w = at::zeros({(int64_t)api.matmul_i8_workspace_size()},
-                  at::TensorOptions().dtype(at::kByte).device(dev));
-    // a buffer made while a graph is captured belongs to that graph
-    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (!known && !PyErr_Occurred()) {
     C10_CUDA_CHECK(cudaStreamIsCapturing(stream, &status));
     if (status != cudaStreamCaptureStatusNone) {
-      stored = 0;
-    } else if (PyObject* o = wrap(w)) {
-      stored = PyDict_SetItem(words, key, o);
-      Py_DECREF(o);
+      Py_DECREF(key);
+      key = Py_BuildValue("(iO)", (int)dev.index(), Py_None);
+      if (!key) throw Refused();
+      known = PyDict_GetItemWithError(words, key);
     }
   }
+  at::Tensor w;
+  if (known) {
+    w = THPVariable_Unpack(known);
+  } else if (!PyErr_Occurred()) {
+    w = status != cudaStreamCaptureStatusNone
+            ? word_beside_capture(dev)
+            : at::zeros({(int64_t)api.matmul_i8_workspace_size()},
+                        at::TensorOptions().dtype(at::kByte).device(dev));
+    PyObject* o = wrap(w);
+    if (o) PyDict_SetItem(words, key, o);
+    Py_XDECREF(o);
+  }
   Py_DECREF(key);
-  if (stored < 0) throw Refused();
+  if (PyErr_Occurred()) throw Refused();
   return w;
 }
 
