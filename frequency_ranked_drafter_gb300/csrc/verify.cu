@@ -27,6 +27,7 @@
 
 #include "cluster.cuh"
 #include "ranges.cuh"
+#include "verify_plan.cuh"
 #include "vt_checks.cuh"
 #include "vt_common.cuh"
 
@@ -35,7 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = kVerifyMaxCluster;
 constexpr int kMaxV = 1 << 19;  // 2^19 probabilities of at most 2^44 stay below 2^63
 constexpr int kBatch = 4;       // 16-byte loads of each row a lane has in flight
 
@@ -271,6 +272,37 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(VerifyArgs a) {
   }
 }
 
+// The largest cluster (a power of two) that the device can hold, asked once: where
+// SMs are shared out or missing, 16 free ones may not lie together.
+vt_status largest_cluster(const DeviceInfo& di, int* largest) {
+  static std::atomic<int> known[64];
+  std::atomic<int>& k = known[di.device & 63];
+  *largest = k.load();
+  if (*largest > 0) return VT_OK;
+  cudaError_t e =
+      cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess)
+    return fail(VT_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+  for (*largest = kMaxCluster; *largest > 1; *largest /= 2) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = *largest;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)*largest);
+    cfg.blockDim = dim3(kThreads);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int active = 0;
+    e = cudaOccupancyMaxActiveClusters(&active, verify_kernel, &cfg);
+    if (e == cudaSuccess && active > 0) break;
+    if (e != cudaSuccess) (void)cudaGetLastError();
+  }
+  k.store(*largest);
+  return VT_OK;
+}
+
 }  // namespace
 }  // namespace vt
 
@@ -304,15 +336,10 @@ extern "C" vt_status vt_verify_draft(const int32_t* draft_ids, const int32_t* n_
     return fail(VT_ERR_INVALID_ARG, "vt_verify_draft: an output overlaps an input or the other");
   DeviceInfo di;
   if (!current_device(&di)) return VT_ERR_CUDA;
-  int C = 1;
-  // CTAs a sequence, each with 1024 ids at least.  An SM holds four of them.  Up
-  // to eight a sequence, two rounds of shorter segments beat one of longer ones
-  // (V = 128256, B = 100: 27.4 us with eight, 31.9 with four; V = 32003, B = 64:
-  // 9.1 and 11.9); sixteen have to fit at once (V = 128256, B = 24: 10.3 us with
-  // sixteen, 14.6 with eight; B = 64: 21.1 and 18.0).
-  while (C < kMaxCluster && V > C * 1024 &&
-         (int64_t)B * C * 2 <= (C < 8 ? 8ll : 4ll) * di.num_sms)
-    C *= 2;
+  int largest;
+  const vt_status st = largest_cluster(di, &largest);
+  if (st != VT_OK) return st;
+  const int C = verify_ctas(B, V, di.num_sms, largest);
   VerifyArgs a;
   a.draft = draft_ids;
   a.n_draft = n_draft;
@@ -331,15 +358,6 @@ extern "C" vt_status vt_verify_draft(const int32_t* draft_ids, const int32_t* n_
   a.u = u;
   a.accepted = n_accepted;
   a.out = out_ids;
-  static std::atomic<uint64_t> wide{0};  // devices whose kernel may have 16 CTAs a cluster
-  const uint64_t bit = 1ull << (di.device & 63);
-  if (!(wide.load() & bit)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess)
-      return fail(VT_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
-    wide.fetch_or(bit);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * C));
   cfg.blockDim = dim3(kThreads);
