@@ -560,7 +560,8 @@ def matmul_i8(Q: torch.Tensor, scale: torch.Tensor, Wq: torch.Tensor,
                                           _i8_words)
     if check:
         if ws is None:
-            ws = _i8_words[Q.device.index, _stream(Q.device)]
+            i = Q.device.index  # (while captured the read is refused, as CUDA refuses it)
+            ws = _i8_words.get((i, _stream(Q.device)), _i8_words.get((i, None)))
         check_error_word("vt_matmul_i8", ws)
     return y
 

@@ -17,7 +17,8 @@
 // there are too few rows to fill the SMs with warps.  The rounding was what
 // bounded it at first: with the exact test behind one branch for a chunk and
 // the maximum taken on packed bits, 32768 gathered rows of 4096 bf16 went from
-// 98.7 to 66.2 us (6.1 TB/s of reads and writes, 0.90 of the measured copy).
+// 98.7 to 66.2 us (6.1 TB/s of reads and writes, 0.90 of the measured copy; rows in
+// order 64.2, fp16 62.8, fp32 100.9 us, two warps a row).
 #include <cuda_fp16.h>
 
 #include "ranges.cuh"

@@ -545,7 +545,8 @@ vt_status vt_quantize_rows(const void* X, int32_t dtype, int64_t V, int32_t d,
  *   ws        (device) vt_matmul_i8_workspace_size() bytes, 256-byte aligned,
  *             zero-filled once before its first use.  It holds nothing but
  *             the error word (byte 128), so calls may share it, concurrent
- *             ones and captured ones too.  The call never clears the word.
+ *             ones and captured ones too; which of them it speaks of is then
+ *             not known.  The call never clears the word.
  *   M == 0 or N == 0 is a valid no-op.
  * ------------------------------------------------------------------------ */
 size_t vt_matmul_i8_workspace_size(void);
@@ -586,6 +587,7 @@ vt_status vt_selftest_matmul_i8(const int8_t* X, const float* x_scale, int32_t M
  *   (sum of kept w_j over j <= i) > u * S; out_ids = t2f[i], or i;
  *   out_probs = p_i.  out_dist[m][i] = p_i.
  *
+ *   Temperatures between 0 and 1e-30 count as 1e-30 in the weights.
  *   T == 0 is greedy: the first maximum, with probability 1.  Logits of -inf
  *   are never drawn; +inf logits share the mass equally.  A row that is all
  *   -inf gives id -1 and probability 0 (and a distribution of zeros); a row
