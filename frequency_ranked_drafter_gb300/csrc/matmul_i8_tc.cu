@@ -383,8 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     bool ok = true;
     for (int i = u; i < total; i += 2) {
-      if (!__all_sync(~0u, await(&raw_full[r.i], r.ph) &&
-                               await(&cv_empty[c.i], c.ph ^ 1u))) {
+      // The converted place first.  The sets take turns at a stage's place when
+      // the places are odd in number, and a parity cannot tell phase k - 2 from
+      // phase k: with the place of stage i - conv free again, every stage up to
+      // that one (of this place too) has landed, so the bytes' phase is the one
+      // waited for.  In the other order a stage could be read before it lay there.
+      if (!__all_sync(~0u, await(&cv_empty[c.i], c.ph ^ 1u) &&
+                               await(&raw_full[r.i], r.ph))) {
         ok = false;
         break;
       }
@@ -445,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = tile == tile0;
         int sum[kBlockM / 32] = {};
         for (; kb < nk; kb += 2) {
-          if (!__all_sync(~0u, await(&raw_full[r.i], r.ph) &&
-                                   await(&cv_empty[c.i], c.ph ^ 1u))) {
+          if (!__all_sync(~0u, await(&cv_empty[c.i], c.ph ^ 1u) &&
+                                   await(&raw_full[r.i], r.ph))) {  // (as W's warps do)
             ok = false;
             break;
           }
@@ -781,6 +786,7 @@ static vt_status launch_tc(const I8Args& g, unsigned* err, long long budget, con
   const int b_bytes = a.conv * a.nt * kStageK * 2 + a.mblocks * a.nt * (int)sizeof(RowInfo) +
                       (a.splits > 1 ? a.nt * a.rt * 4 : 0);
   a.stages = std::min(kMaxStages, (di.max_smem_optin - 2048 - b_bytes) / stage_bytes);
+  // (the converting warps' waits rely on a.conv <= a.stages, or two stages)
   if (a.stages < 2) return fail(VT_ERR_UNSUPPORTED, "vt_matmul_i8: stages do not fit");
   CUtensorMap tmW, tmX;
   if (!byte_map(&tmW, g.W, g.N, g.d, a.rt) || !byte_map(&tmX, g.X, g.M, g.d, a.nt))
