@@ -8,8 +8,9 @@
 // x * (1 / s)) is off by at most one and only next to a half, and
 // e = x - r * s, one fused multiply-add, is exact there (both terms are
 // multiples of half the last place of s and |e| < s), so comparing |e| with
-// s / 2 settles the integer.  Every build and every order of work gives the
-// same bytes.
+// s / 2 settles the integer.  (s / 2 has to be an fp32 number for that: a row whose
+// scale is below 2^-125 is multiplied by 2^24 first.)  Every build and every order
+// of work gives the same bytes.
 //
 // Bound by HBM: R * d * (size + 1) bytes, each value read once.  A row is
 // held in registers between the maximum and the rounding (16 chunks of 16
@@ -58,6 +59,17 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[DT == VT_FP32 
       x[2 * i + 1] = f.y;
     }
   }
+}
+
+// A chunk of tiny values, times 2^24 (exact in either type).
+template <int DT>
+__device__ __forceinline__ uint4 times_2_24(const uint4& v) {
+  auto up = [](uint32_t w) {
+    if constexpr (DT == VT_FP32) return __float_as_uint(__uint_as_float(w) * 0x1p24f);
+    return (__float_as_uint(bf16hi(w) * 0x1p24f) & 0xffff0000u) |
+           __float_as_uint(bf16lo(w) * 0x1p24f) >> 16;
+  };
+  return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
 }
 
 // Nearest integers to x / s in the low bytes (two's complement); inv = 1 / s,
@@ -153,7 +165,13 @@ __global__ void __launch_bounds__(kQThreads, 2) quantize_rows_kernel(QuantArgs a
     // product with it is NaN
     const bool finite = mx < 0x7f800000u;
     const float s = fmaxf((finite ? __uint_as_float(mx) : 0.f) * (1.f / 127.f), 0x1p-126f);
-    const float inv = __fdiv_rn(1.f, s), half = 0.5f * s;
+    float step = s;
+    if (DT != VT_FP16 && s < 0x1p-125f) {
+      step = s * 0x1p24f;
+#pragma unroll
+      for (int j = 0; j < kQChunks; ++j) v[j] = times_2_24<DT>(v[j]);
+    }
+    const float inv = __fdiv_rn(1.f, step), half = 0.5f * step;
 #pragma unroll
     for (int j = 0; j < kQChunks; ++j) {
       const int c = lane + 32 * part + kStep * j;
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(kQThreads, 2) quantize_rows_kernel(QuantArgs a
       float x[kVals];
       unpack<DT>(v[j], x);
       uint32_t q[kVals];
-      to_int8<kVals>(x, s, inv, half, q);
+      to_int8<kVals>(x, step, inv, half, q);
       if (!finite) {
 #pragma unroll
         for (int i = 0; i < kVals; ++i) q[i] = 0u;
