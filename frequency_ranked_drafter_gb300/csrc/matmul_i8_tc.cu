@@ -38,7 +38,7 @@
 // 3.8 TB/s, 0.56 of the measured copy): the chain of a stage, whose bytes are
 // converted, multiplied and its place freed in some 3000 clocks with three
 // stages under way.  With 128 rows of X and more (N = 128256, d = 2048: M = 128
-// 94 us, 720 TFLOP/s; M = 256 187 us) the same chain, longer by X's bytes, which
+// 94 us, 720 TFLOP/s; M = 256 185 us) the same chain, longer by X's bytes, which
 // pass through shared memory four times (in, out, back as fp16, to the MMA).  Measured and not used: 64 k a
 // stage (M = 60: 50 us), tensor loads ahead of the ring into L2 (34 to 37 us
 // where streaming alone took 29), stores of 16 columns to tensor memory and W
